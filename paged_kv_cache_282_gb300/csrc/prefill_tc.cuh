@@ -31,8 +31,10 @@
 // tile, so the exponentials need no pass over S first (a row's first tile has
 // one, for its maximum).  When a tile's weights sum to more than 1024, m moves
 // by the sum's logarithm and the row's O and sum are rescaled before the next
-// tile: rare after the first tiles.  Any weight that fits fp32 and bf16 keeps
-// its relative precision; one that does not makes O infinite.
+// tile: rare after the first tiles.  Logits that rise by more than about 87
+// from one tile to the next leave fp32's range: the tile's sum is infinite, or
+// the factor for what came before no normal number.  The factor is then NaN,
+// which stays in the row's O and sum.
 //
 // One-byte pools: logits are scaled by the token's K scale in fp32, weights
 // by its V scale before their rounding to bf16; per-channel scales (powers of
@@ -40,8 +42,8 @@
 //
 // Keys a row does not keep get weight 0, but 0 times a NaN or infinity of V
 // would still reach the row.  Slots past the sequence's end (never written)
-// are zeroed in shared memory; for written ones, a row whose O is not finite
-// is computed again key by key on the CUDA cores.
+// are zeroed in shared memory; for written ones, a row whose O or sum is not
+// finite is computed again key by key on the CUDA cores.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -838,6 +840,15 @@ __device__ void softmax_role(const PrefillTCParams& p, const Ctx<KV, D>& x, uint
       l += tile;
       return tile > 1024.0f ? hw_log2(tile) : 0.0f;
     };
+    // Moves the reference by over > 0; the factor of what the row holds, from
+    // the step that m really took.  NaN where it would flush to 0: weights of
+    // the tile may have left fp32's range, so the row is computed again.
+    auto move = [&](float over) {
+      const float from = m;
+      m += over;
+      const float f = hw_exp2(from - m);
+      return f == 0.0f ? __int_as_float(0x7fffffff) : f;
+    };
     for (int k = pc.k0; k < k1; ++k) {
       if (!part.has(k)) {
         if constexpr (C::kOneByte) {  // in step with the ring, so that no arrival counts for a later round
@@ -879,8 +890,7 @@ __device__ void softmax_role(const PrefillTCParams& p, const Ctx<KV, D>& x, uint
       tmem_load32(ts, s);
       if (rare) {
         if (__any_sync(kFull, over > 0.0f)) {
-          const float f = over > 0.0f ? hw_exp2(-over) : 1.0f;
-          m += over;
+          const float f = over > 0.0f ? move(over) : 1.0f;
           l *= f;
 #pragma unroll 1
           for (int b = 0; b < D; b += 16) {  // O, which holds the tiles before this one
@@ -978,8 +988,7 @@ __device__ void softmax_role(const PrefillTCParams& p, const Ctx<KV, D>& x, uint
       }
     }
 
-    const float over = any ? settle() : 0.0f, f = over > 0.0f ? hw_exp2(-over) : 1.0f;
-    m += over;
+    const float over = any ? settle() : 0.0f, f = over > 0.0f ? move(over) : 1.0f;
     l *= f;
     // output row (or partial record's row) of this warp's row r32
     const int per = kPreRows >> p.g_log2, base = (warp & 3) * 32;
@@ -1005,7 +1014,7 @@ __device__ void softmax_role(const PrefillTCParams& p, const Ctx<KV, D>& x, uint
       }
     };
     if (valid_row) row_stats(lane, m, l);
-    float bad = 0.0f;  // NaN once some O is not finite
+    float bad = l * 0.0f;  // NaN once the sum or some O is not finite
     if (any) {
       if (!x.wait(x.o_full(i), o_round, p.status)) return;
       o_round ^= 1;
