@@ -244,8 +244,9 @@ typedef struct {
  *   q_out      device [token][n_heads][D]; may be q itself when q_stride is
  *              n_heads * D
  *   positions  device int32 [token], or NULL: each token's index in its
- *              sequence.  A position outside the table sets the status word
- *              (PKV_ERR_DEVICE_ASSERT) and none of the token's rows is written.
+ *              sequence; not read when rope->rot_dim is 0.  A position outside
+ *              the table sets the status word (PKV_ERR_DEVICE_ASSERT) and none
+ *              of the token's rows is written.
  * Errors: as pkv_append; PKV_ERR_INVALID_ARG also when q_out overlaps an
  * input, a default position is past the table, or the current device is not
  * the pool's; PKV_ERR_UNSUPPORTED for a rot_dim as above, or while `stream` is

@@ -332,7 +332,7 @@ class PagedKVCache:
             raise ValueError(f"positions must be contiguous int32 [{ntok}] on {dev}")
         _abi.check(self.lib.pkv_append_rope(
             self._h, _stream_ptr(stream), ids.size, _ptr(ids), _ptr(cnt), rope._check(self.head_dim, dt, dev),
-            positions.data_ptr() if positions is not None else None, pq or None, sq, po or None, pk or None, sk, pv or None,
+            positions.data_ptr() if positions is not None and rope.rot_dim > 0 else None, pq or None, sq, po or None, pk or None, sk, pv or None,
             sv))
         return q_out
 
@@ -364,7 +364,7 @@ class PagedKVCache:
                                        or not positions.is_contiguous() or positions.device != dev):
             raise ValueError(f"positions must be contiguous int32 [{n}] on {dev}")
         _abi.check(self.lib.pkv_qk_norm_rope(self._h, _stream_ptr(stream), n or 0, rope._check(self.head_dim, dt, dev),
-                                             positions.data_ptr() if positions is not None else None, *args))
+                                             positions.data_ptr() if n and rope.rot_dim > 0 else None, *args))
         return (q_out if q is not None else None), (k_out if k is not None else None)
 
     def prefill(self, seq_ids, q_lens, q, scale: float | None = None, mask: str = "full", num_sinks: int = 0,

@@ -1948,6 +1948,7 @@ void fill_rope(const pkv_pool* p, const pkv_rope* rope, RopeArgs& a) {
   a.n_positions = rope->n_positions;
   a.rot = rope->rot_dim;
   a.interleaved = rope->interleaved != 0;
+  a.positions = nullptr;  // not read without a rotation
   a.k_pool = p->buf.k_pool;
   a.v_pool = p->buf.v_pool;
   a.k_scale = p->buf.k_scale;
@@ -2609,7 +2610,8 @@ pkv_status pkv_append_rope(pkv_pool* p, void* stream, int32_t n, const int32_t* 
         return fail(PKV_ERR_INVALID_ARG, "sequence %d: position %lld is past the table's %d", ids[i],
                     (long long)A.len[ids[i]] + counts[i] - 1, rope->n_positions);
     }
-    if (positions && ((size_t)positions & 3)) return fail(PKV_ERR_INVALID_ARG, "positions must be 4-byte aligned");
+    if (positions && rope->rot_dim > 0 && ((size_t)positions & 3))
+      return fail(PKV_ERR_INVALID_ARG, "positions must be 4-byte aligned");
     if (ntok > 0) {
       const int64_t qw = (int64_t)c.n_heads * c.head_dim, kw = (int64_t)c.n_kv_heads * c.head_dim;
       const Rows rk{"k", k, k_stride, kw}, rv{"v", v, v_stride, kw};
@@ -2670,7 +2672,7 @@ pkv_status pkv_append_rope(pkv_pool* p, void* stream, int32_t n, const int32_t* 
       a.n_patches = (int)np;
       a.tokens = nullptr;
       a.patches = nullptr;
-      a.positions = positions ? positions + t0 : nullptr;
+      if (positions && a.rot > 0) a.positions = positions + t0;
       a.q = (const char*)q + t0 * q_stride * es;
       a.q_out = (char*)q_out + t0 * a.q_out_stride * es;
       a.k = (const char*)k + t0 * k_stride * es;
@@ -2758,7 +2760,7 @@ pkv_status pkv_qk_norm_rope(pkv_pool* p, void* stream, int32_t n_tokens, const p
     const int64_t chunk = rope_chunk(a.H + a.Hk);
     for (int64_t t0 = 0; t0 < n_tokens; t0 += chunk) {
       a.n_tokens = (int)std::min<int64_t>(chunk, n_tokens - t0);
-      a.positions = positions ? positions + t0 : nullptr;
+      if (positions && a.rot > 0) a.positions = positions + t0;
       a.q = (const char*)q + t0 * q_stride * es;
       a.q_out = (char*)q_out + t0 * q_out_stride * es;
       a.k = (const char*)k + t0 * k_stride * es;

@@ -366,3 +366,30 @@ def test_binding_refusals():
     cache.append_rope([], k[:0], v[:0], rope, counts=[])
     cache.sync_status()
     assert cache.seq_len(s) == 3 and pkv.version()
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+def test_positions_are_not_read_without_a_rotation(kv):
+    """The library is given an address that no int32 can be read from."""
+    cache = PagedKVCache(4, 4, 2, 64, 1, 4, kv_dtype=kv)
+    w = _weights(64, BF, 7)
+    rope = Rope(1, 0, q_weight=w[0], k_weight=w[1])
+    x = _rand((5, 8, 64), BF, 4).cuda()
+    y, mag = _rotated(x[:, :4].cpu(), w[0].cpu(), torch.zeros(5), 0, False)
+    q = torch.empty((5, 4, 64), dtype=BF, device="cuda")
+    k = torch.empty((5, 2, 64), dtype=BF, device="cuda")
+    odd = torch.zeros(64, dtype=torch.uint8, device="cuda").data_ptr() + 1
+    pkv._abi.check(cache.lib.pkv_qk_norm_rope(cache.handle, pkv._stream_ptr(None), 5, rope._ref, odd, x.data_ptr(), 8 * 64,
+                                              q.data_ptr(), 4 * 64, x.data_ptr() + 4 * 64 * 2, 8 * 64, k.data_ptr(), 2 * 64))
+    cache.sync_status()
+    _close(q, y, mag, BF)
+    s, one = np.array([cache.seq_add()], np.int32), np.array([5], np.int32)
+    q2 = torch.empty_like(q)
+    pkv._abi.check(cache.lib.pkv_append_rope(cache.handle, pkv._stream_ptr(None), 1, s.ctypes.data, one.ctypes.data, rope._ref, odd,
+                                             x.data_ptr(), 8 * 64, q2.data_ptr(), x.data_ptr() + 4 * 64 * 2, 8 * 64,
+                                             x.data_ptr() + 6 * 64 * 2, 8 * 64))
+    cache.sync_status()
+    assert torch.equal(q2, q)
+    # the binding: positions on the host, and too few of them
+    for positions in (torch.arange(5), torch.zeros(1, dtype=torch.int32, device="cuda"), None):
+        assert torch.equal(cache.qk_norm_rope(x[:, :4], None, positions, rope)[0], q)

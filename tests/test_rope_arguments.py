@@ -1,0 +1,53 @@
+"""What the binding of the rotation and prefill calls hands to the library, seen through a library that only records it."""
+import types
+
+import pytest
+import torch
+
+import paged_kv_cache_282_gb300 as pkv
+from paged_kv_cache_282_gb300 import PagedKVCache, Rope
+
+BF = torch.bfloat16
+H, HK, D = 4, 2, 64
+
+
+class Recorder:
+    """Stands for the library in the calls that need a device; the rest goes to the library itself."""
+
+    def __init__(self, lib, *names):
+        self.lib, self.names, self.calls = lib, names, []
+
+    def __getattr__(self, name):
+        if name not in self.names:
+            return getattr(self.lib, name)
+
+        def call(*args):
+            self.calls.append((name, args))
+            return 0
+        return call
+
+
+def _cache(*names):
+    c = PagedKVCache(8, H, HK, D, 2, 4, host_only=True)
+    c.device = torch.device("cpu")
+    c.k_pool = torch.empty(8, HK, 16, D, dtype=BF)  # the binding asks it for the device
+    c.lib = Recorder(c.lib, *names)
+    return c
+
+
+STREAM = types.SimpleNamespace(cuda_stream=0)
+
+
+@pytest.mark.parametrize("rot,positions", [(0, torch.arange(3)), (0, torch.zeros(1, dtype=torch.int32)), (0, None),
+                                           (32, torch.arange(3, dtype=torch.int32))])
+def test_positions_are_handed_over_only_where_something_rotates(rot, positions):
+    """Without a rotation they are not read, so anything may be given: it must not reach the device."""
+    c = _cache("pkv_qk_norm_rope")
+    rope = Rope(16, rot, device="cpu")
+    q, k = torch.zeros(3, H, D, dtype=BF), torch.zeros(3, HK, D, dtype=BF)
+    c.qk_norm_rope(q, k, positions, rope, q_out=q, k_out=k, stream=STREAM)
+    assert c.lib.calls[0][1][4] == (positions.data_ptr() if rot else None)
+    c = _cache("pkv_append_rope")
+    if rot or positions is None:
+        c.append_rope([0], k, k, rope, counts=[3], positions=positions, stream=STREAM)
+        assert c.lib.calls[0][1][6] == (positions.data_ptr() if rot else None)
