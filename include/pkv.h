@@ -260,7 +260,7 @@ pkv_status pkv_append_rope(pkv_pool* pool, void* stream, int32_t n_seqs, const i
  * (device int32 [n_tokens]; not read when rope->rot_dim is 0): q [token]
  * [n_heads][D] into q_out, k [token][n_kv_heads][D] into k_out, rows and
  * strides as in pkv_append_rope (fp32 rows on an fp32 pool, else bf16).  q or
- * k may be NULL.  An output may be its input (same stride), also inside one
+ * k may be NULL.  An output may be its own input (same stride), also inside one
  * packed tensor; other overlaps are PKV_ERR_INVALID_ARG.  The pool gives the
  * shapes and the status word; its cache is not touched.  The call may be
  * captured into a graph (not while its launches are timed, pkv_timing_enable). */

@@ -340,7 +340,7 @@ class PagedKVCache:
         """Per-head norms and rotation of queries [tokens][n_heads][head_dim]
         and keys [tokens][n_kv_heads][head_dim] (either may be None) at
         positions (device int32), without storing; returns (q_out, k_out).
-        Outputs may be the inputs themselves."""
+        An output may be its own input."""
         import torch
         dt, dev = self._row_dtype, self.k_pool.device
         args, n = [], None

@@ -1914,9 +1914,11 @@ pkv_status check_rows(const Rows& r, int64_t n, int es) {
   return PKV_OK;
 }
 
-// `out` may be `in` itself (same place, same stride) but not overlap it otherwise.
-pkv_status check_overlap(const Rows& out, const Rows& in, int64_t n, int es) {
-  if (out.ptr == in.ptr && out.stride == in.stride && out.width == in.width) return PKV_OK;
+// `out` must not overlap `in`.  With own (a row of `out` is made from that row
+// of `in` alone, by the threads that read it) it may be `in` itself, in the
+// same place with the same stride.
+pkv_status check_overlap(const Rows& out, const Rows& in, int64_t n, int es, bool own = false) {
+  if (own && out.ptr == in.ptr && out.stride == in.stride) return PKV_OK;
   if (out.begin() < in.end(n, es) && in.begin() < out.end(n, es))
     return fail(PKV_ERR_INVALID_ARG, "%s overlaps %s", out.what, in.what);
   return PKV_OK;
@@ -2621,7 +2623,8 @@ pkv_status pkv_append_rope(pkv_pool* p, void* stream, int32_t n, const int32_t* 
         const Rows rq{"q", q, q_stride, qw}, ro{"q_out", q_out, qw, qw};
         if (pkv_status r = check_rows(rq, ntok, es)) return r;
         if (pkv_status r = check_rows(ro, ntok, es)) return r;
-        for (const Rows* in : {&rq, &rk, &rv})
+        if (pkv_status r = check_overlap(ro, rq, ntok, es, /*own=*/true)) return r;
+        for (const Rows* in : {&rk, &rv})
           if (pkv_status r = check_overlap(ro, *in, ntok, es)) return r;
       }
     }
@@ -2720,9 +2723,9 @@ pkv_status pkv_qk_norm_rope(pkv_pool* p, void* stream, int32_t n_tokens, const p
       for (const Rows* r : {&rk, &rko})
         if (pkv_status st2 = check_rows(*r, n_tokens, es)) return st2;
     if (q)
-      if (pkv_status r = check_overlap(rqo, rq, n_tokens, es)) return r;
+      if (pkv_status r = check_overlap(rqo, rq, n_tokens, es, /*own=*/true)) return r;
     if (k)
-      if (pkv_status r = check_overlap(rko, rk, n_tokens, es)) return r;
+      if (pkv_status r = check_overlap(rko, rk, n_tokens, es, /*own=*/true)) return r;
     // In place inside one packed tensor the query rows interleave with the
     // key rows (their ranges overlap, their rows do not); any other overlap
     // between the two sides is refused.
@@ -2736,8 +2739,7 @@ pkv_status pkv_qk_norm_rope(pkv_pool* p, void* stream, int32_t n_tokens, const p
       if (!(packed && apart)) {
         if (pkv_status r = check_overlap(rqo, rk, n_tokens, es)) return r;
         if (pkv_status r = check_overlap(rko, rq, n_tokens, es)) return r;
-        if (rqo.begin() < rko.end(n_tokens, es) && rko.begin() < rqo.end(n_tokens, es))
-          return fail(PKV_ERR_INVALID_ARG, "q_out overlaps k_out");
+        if (pkv_status r = check_overlap(rqo, rko, n_tokens, es)) return r;
       }
     }
     if (pkv_status r = check_call(p, st, "pkv_qk_norm_rope", PKV_KERNEL_QK_ROPE)) return r;
