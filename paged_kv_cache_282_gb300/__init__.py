@@ -38,6 +38,23 @@ def _stream_ptr(stream) -> int:
     return int(stream.cuda_stream)
 
 
+def _on(stream):
+    """torch's context of `stream` (a torch stream, or anything with its handle)."""
+    import torch
+    return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream)
+                             else torch.cuda.ExternalStream(int(stream.cuda_stream)))
+
+
+def _empty(shape, dtype, device, stream):
+    """Memory for a call on `stream` (None: the current one), of that stream:
+    once dropped it is handed on behind the work that is queued there."""
+    import torch
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with _on(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _i32_array(values) -> np.ndarray:
     return np.ascontiguousarray(np.asarray(values, dtype=np.int32))
 
@@ -128,7 +145,11 @@ class PagedKVCache:
     methods that forward to the C ABI.
 
     kv_dtype: "fp32" | "bf16" | "fp8" | "int8".  host_only=True creates the allocator
-    without device buffers (allocator calls only)."""
+    without device buffers (allocator calls only).
+
+    A pool's device work runs in call order: whoever passes `stream` to its
+    calls orders the streams.  What append_rope, qk_norm_rope and prefill
+    allocate (outputs, scratch) is memory of the call's stream."""
 
     def __init__(self, num_blocks: int, n_heads: int, n_kv_heads: int, head_dim: int, max_seqs: int,
                  max_blocks_per_seq: int, kv_dtype: str = "bf16", alloc_seed: int = 0, free_order=None,
@@ -145,6 +166,7 @@ class PagedKVCache:
         self._h = ctypes.c_void_p()
         self.host_only = host_only
         self._workspace = None
+        self._prefill_scratch = {}  # by stream handle: calls on two streams must not share it
         if host_only:
             _abi.check(self.lib.pkv_pool_create(ctypes.byref(self.cfg), None, ctypes.byref(self._h)))
             return
@@ -323,7 +345,7 @@ class PagedKVCache:
         if q is not None:
             pq, nq, sq = _token_rows(q, self.n_heads, self.head_dim, dt, dev, "q")
             if q_out is None:
-                q_out = torch.empty(q.shape, dtype=dt, device=dev)
+                q_out = _empty(q.shape, dt, dev, stream)
             po, no, so = _token_rows(q_out, self.n_heads, self.head_dim, dt, dev, "q_out")
             if nq != ntok or no != ntok or so != self.n_heads * self.head_dim:
                 raise ValueError(f"q of {nq} and a contiguous q_out of {no} tokens for {ntok}")
@@ -349,7 +371,7 @@ class PagedKVCache:
                 args += [None, 0, None, 0]
                 continue
             if out is None:
-                out = torch.empty(x.shape, dtype=dt, device=dev)
+                out = _empty(x.shape, dt, dev, stream)
             px, nx, sx = _token_rows(x, heads, self.head_dim, dt, dev, name)
             po, no, so = _token_rows(out, heads, self.head_dim, dt, dev, name + "_out")
             if no != nx or (n is not None and nx != n):
@@ -377,22 +399,23 @@ class PagedKVCache:
         ids, lens = _i32_array(seq_ids), _i32_array(q_lens)
         pq, n, sq = _token_rows(q, self.n_heads, self.head_dim, dt, dev, "q")
         if out is None:
-            out = torch.empty(q.shape, dtype=dt, device=dev)
+            out = _empty(q.shape, dt, dev, stream)
         po, no, so = _token_rows(out, self.n_heads, self.head_dim, dt, dev, "out")
         if lens.size != ids.size or int(lens.sum()) != n or no != n:
             raise ValueError(f"{ids.size} sequences, {lens.size} q_lens of {int(lens.sum())} tokens, q of {n}, out of {no}")
         if sq != self.n_heads * self.head_dim or so != sq:
             raise ValueError("q and out must be contiguous")
         if lse is None:
-            lse = torch.empty((n, self.n_heads), dtype=torch.float32, device=dev)
+            lse = _empty((n, self.n_heads), torch.float32, dev, stream)
         elif lse is not False and (lse.dtype != torch.float32 or lse.device != dev or lse.numel() != n * self.n_heads
                                    or not lse.is_contiguous()):
             raise ValueError(f"lse must be contiguous float32 [{n}][{self.n_heads}] on {dev}")
         if scale is None:
             scale = 1.0 / math.sqrt(self.head_dim)
-        ws = workspace if workspace is not None else self._prefill_workspace()
+        at = _stream_ptr(stream)
+        ws = workspace if workspace is not None else self._prefill_workspace(at, stream)
         _abi.check(self.lib.pkv_prefill_attn(
-            self._h, _stream_ptr(stream), ids.size, _ptr(ids), _ptr(lens), pq or None, float(scale), MASKS[mask],
+            self._h, at, ids.size, _ptr(ids), _ptr(lens), pq or None, float(scale), MASKS[mask],
             num_sinks, window, po or None, lse.data_ptr() if lse is not False else None,
             ws.data_ptr() if ws is not None else None, ws.numel() * ws.element_size() if ws is not None else 0))
         return out, lse
@@ -402,15 +425,14 @@ class PagedKVCache:
         _abi.check(self.lib.pkv_prefill_workspace_size(self._h, ctypes.byref(b)))
         return b.value
 
-    def _prefill_workspace(self):
-        import torch
-        if getattr(self, "_prefill_bytes", None) is None:
-            self._prefill_bytes = self.prefill_workspace_bytes()
-        if self._prefill_bytes == 0:
-            return None
-        if self._workspace is None or self._workspace.numel() < self._prefill_bytes:
-            self._workspace = torch.empty(self._prefill_bytes, dtype=torch.uint8, device=self.device)
-        return self._workspace
+    def _prefill_workspace(self, at: int, stream):
+        """The scratch of prefill calls on the stream with handle `at`: one
+        tensor a stream, of that stream, kept as long as the cache."""
+        if at not in self._prefill_scratch:
+            import torch
+            need = self.prefill_workspace_bytes()
+            self._prefill_scratch[at] = _empty(need, torch.uint8, self.device, stream) if need else None
+        return self._prefill_scratch[at]
 
     def workspace_bytes(self, n_seqs: int, num_splits: int = 0) -> int:
         b = ctypes.c_size_t()

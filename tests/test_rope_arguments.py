@@ -51,3 +51,43 @@ def test_positions_are_handed_over_only_where_something_rotates(rot, positions):
     if rot or positions is None:
         c.append_rope([0], k, k, rope, counts=[3], positions=positions, stream=STREAM)
         assert c.lib.calls[0][1][6] == (positions.data_ptr() if rot else None)
+
+
+def test_prefill_scratch_belongs_to_the_stream(monkeypatch):
+    """Calls on two streams, and decode, never get the same scratch; nothing that a call allocates is of another stream."""
+    c = _cache("pkv_prefill_attn", "pkv_append_rope", "pkv_qk_norm_rope")
+    inside = []
+
+    class On:
+        def __init__(self, stream):
+            self.stream = stream
+
+        def __enter__(self):
+            inside.append(self.stream)
+
+        def __exit__(self, *a):
+            inside.append(None)
+
+    monkeypatch.setattr(pkv, "_on", On, raising=False)
+    empty, made = torch.empty, []
+
+    def note(*a, **kw):
+        made.append(inside[-1] if inside else None)
+        return empty(*a, **kw)
+    monkeypatch.setattr(torch, "empty", note)
+    streams = [types.SimpleNamespace(cuda_stream=i) for i in (1, 2, 1, 2)]
+    q = torch.zeros(2, H, D, dtype=BF)
+    decode = c.workspace(1)
+    made.clear()
+    used = []
+    for s in streams:
+        out, lse = c.prefill([0], [2], q, stream=s)
+        used.append(c.lib.calls[-1][1][12])
+        assert c.lib.calls[-1][1][1] == s.cuda_stream
+    assert used[0] == used[2] != used[1] == used[3] and decode.data_ptr() not in used
+    assert c.workspace(1) is decode
+    k = torch.zeros(2, HK, D, dtype=BF)
+    rope = Rope(16, 0, device="cpu")
+    c.append_rope([0], k, k, rope, counts=[2], q=q, stream=streams[0])
+    c.qk_norm_rope(q, k, None, rope, stream=streams[1])
+    assert [s.cuda_stream for s in made] == [1, 1, 1, 2, 2, 2, 1, 1, 2, 2, 1, 2, 2]
