@@ -393,3 +393,37 @@ def test_positions_are_not_read_without_a_rotation(kv):
     # the binding: positions on the host, and too few of them
     for positions in (torch.arange(5), torch.zeros(1, dtype=torch.int32, device="cuda"), None):
         assert torch.equal(cache.qk_norm_rope(x[:, :4], None, positions, rope)[0], q)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+def test_long_append_on_another_stream_with_own_frequencies(kv):
+    """More tokens than travel in the kernel's parameters (they are staged and uploaded) behind earlier work of the stream,
+    queries among them."""
+    cache = PagedKVCache(64, 8, 4, 128, 2, 26, kv_dtype=kv)
+    s = cache.seq_add()
+    f = [1.0 / (1 + i) for i in range(32)]
+    rope = Rope(500, 64, frequencies=f)
+    x = _rand((400, 16, 128), BF, 3)
+    side = torch.cuda.Stream()
+    xd = torch.zeros((400, 16, 128), dtype=BF, device="cuda")
+    host = x.pin_memory()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        y = torch.zeros(1 << 26, device="cuda")
+        for _ in range(20):
+            y += 1.0
+        xd.copy_(host, non_blocking=True)  # the rows arrive there only now
+    cache.append_rope([s], xd[:100, 8:12], xd[:100, 12:], rope, counts=[100], stream=side)
+    q = cache.append_rope([s], xd[100:, 8:12], xd[100:, 12:], rope, counts=[300], q=xd[100:, :8], stream=side)
+    cache.sync_status(side)
+    side.synchronize()
+    turned = x.double()
+    for i, fi in enumerate(f):
+        t = torch.arange(400).double() * fi
+        a, b = x[..., i].double(), x[..., i + 32].double()
+        turned[..., i] = a * t.cos()[:, None] - b * t.sin()[:, None]
+        turned[..., i + 32] = b * t.cos()[:, None] + a * t.sin()[:, None]
+    mag = 2 * x.double().abs().amax(-1, keepdim=True).expand(turned.shape)
+    _close(q, turned[100:, :8], mag[100:, :8], BF)
+    for got, y, m in zip(_rows(cache, s, 0, 400), (turned[:, 8:12], x[:, 12:].double()), (mag[:, 8:12], x[:, 12:].double().abs())):
+        _check_rows(cache, got, y, m)
