@@ -200,7 +200,7 @@ __global__ void prefill_simple_kernel(const PrefillSimpleParams p) {
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;
 #pragma unroll
   for (int e = 0; e < E; ++e) {
-    o[e] *= inv;
+    o[e] = l == 0.0f ? 0.0f : o[e] * inv;  // (weights of zero: o may be NaN)
     if (KV >= 2 && p.v_channel != nullptr) o[e] *= p.v_channel[g * D + lane * E + e];
   }
   if constexpr (KV == 0) {

@@ -1064,7 +1064,7 @@ __device__ void softmax_role(const PrefillTCParams& p, const Ctx<KV, D>& x, uint
         if (rec != nullptr)
           reinterpret_cast<float*>(to1)[lane + 32 * e] = o[e];
         else
-          reinterpret_cast<__nv_bfloat16*>(to1)[lane + 32 * e] = __float2bfloat16_rn(o[e] * inv1);
+          reinterpret_cast<__nv_bfloat16*>(to1)[lane + 32 * e] = __float2bfloat16_rn(l1 == 0.0f ? 0.0f : o[e] * inv1);
       }
       if (lane == 0) row_stats(src, m1, l1);
     }
