@@ -283,7 +283,8 @@ pkv_status pkv_prefill_workspace_size(const pkv_pool* pool, size_t* bytes_out);
  * lse = -inf.  A key that a query does not keep does not reach its result,
  * whatever its K and V hold (next to a NaN or an infinity in V, or where its
  * logits rise by more than about 80 from one 128 keys to the next, a query
- * may be evaluated key by key: the same result up to rounding).  Accumulation,
+ * may be evaluated key by key: the same result up to rounding, a query some
+ * hundred times slower).  Accumulation,
  * softmax and lse are fp32; on the tensor cores (every pool but fp32) each
  * weight, times its V scale, is rounded to bf16 for the product with V, but
  * not in a call of at most 1024 query rows (tokens times heads) of which none
@@ -501,9 +502,9 @@ pkv_status pkv_timing_enable(pkv_pool* pool, int32_t kernel_mask);
 pkv_status pkv_timing_read(pkv_pool* pool, double* total_ms_out /* [PKV_KERNEL_COUNT] */,
                            int64_t* launches_out /* [PKV_KERNEL_COUNT] */);
 /* Bound (ns, within [1 ms, 60 s]; default 4 s) of every wait of the decode
- * kernel on its shared-memory stages, of the prefill kernel's waits (some of
- * which last as long as it evaluates rows key by key, see pkv_prefill_attn),
- * and of the keep-set selection's waits on the score rows it streams into
+ * kernel on its shared-memory stages, of the prefill kernel's waits (not
+ * counting the time in which it evaluates rows key by key, see
+ * pkv_prefill_attn), and of the keep-set selection's waits on the score rows it streams into
  * shared memory.  A wait that runs out sets
  * PKV_ERR_TIMEOUT in the status word; the warp (decode) or block (selection;
  * its keep_count is then 0) waits for its own copies in flight (bounded

@@ -34,7 +34,7 @@ def _deps():
     files = [os.path.join(CSRC, s) for s in SOURCES]
     files += [os.path.join(CSRC, "pkv_internal.h"), os.path.join(CSRC, "async_copy.cuh"),
               os.path.join(CSRC, "decode_tc.cuh"), os.path.join(CSRC, "prefill_tc.cuh"),
-              os.path.join(CSRC, "tensor_core.cuh"), os.path.join(INCLUDE, "pkv.h"), __file__]
+              os.path.join(CSRC, "tensor_core.cuh"), os.path.join(CSRC, "stored.cuh"), os.path.join(INCLUDE, "pkv.h"), __file__]
     return files
 
 

@@ -50,6 +50,7 @@
 #include <cuda_fp8.h>
 
 #include "pkv_internal.h"
+#include "stored.cuh"
 #include "tensor_core.cuh"
 
 namespace pkv {
@@ -101,7 +102,7 @@ template <int KV, int D>
 struct Ctx {
   using C = PC<KV, D>;
   uint32_t base;  // of shared memory, on a 1024-byte boundary
-  volatile int* abort;
+  volatile int* abort;  // [0]: a wait ran out; [1]: key tiles that rows were computed over key by key
   uint64_t limit_ns;
   __device__ uint32_t q(int tile) const { return base + C::kQ + tile * C::kOperand; }
   __device__ uint32_t stage(int s) const { return base + C::kStage + s * C::kOperand; }
@@ -124,16 +125,23 @@ struct Ctx {
   __device__ uint32_t idle() const { return bar(C::kNumBars - 1); }     // products done, after a failed wait
 
   // Waits for phase `parity`; false when the limit ran out here or elsewhere
-  // in the CTA (every role then leaves).
+  // in the CTA (every role then leaves).  Rows computed key by key can take
+  // longer than the limit: as long as they go on, the time starts anew.
   __device__ bool wait_one(uint32_t bar, uint32_t parity, int32_t* status) const {
     if (mbar_try_wait(bar, parity)) return true;
-    const uint64_t t0 = global_timer();
+    uint64_t t0 = global_timer();
+    int steps = abort[1];
     for (uint32_t it = 1;; ++it) {
       if (mbar_try_wait(bar, parity)) return true;
       if ((it & 63) == 0) {
-        if (*abort) return false;
+        if (abort[0]) return false;
         if (global_timer() - t0 > limit_ns) {
-          *abort = 1;
+          if (abort[1] != steps) {
+            steps = abort[1];
+            t0 = global_timer();
+            continue;
+          }
+          abort[0] = 1;
           atomicOr(status, kStatusTimeout);
           return false;
         }
@@ -635,65 +643,134 @@ __device__ void widen_role(const PrefillTCParams& p, const Ctx<KV, D>& x, int fi
 
 // ---- softmax, output -----------------------------------------------------------
 
-template <int KV>
-__device__ __forceinline__ float stored(const void* pool, size_t i) {
-  if constexpr (KV == 1) return __bfloat162float(static_cast<const __nv_bfloat16*>(pool)[i]);
-  if constexpr (KV == 2)
-    return __half2float(__half(__nv_cvt_fp8_to_halfraw(static_cast<const uint8_t*>(pool)[i], __NV_E4M3)));
-  return (float)static_cast<const int8_t*>(pool)[i];
-}
+__device__ __forceinline__ float row_lse(float m, float l) { return l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2; }
 
-// One query row over the piece's key tiles, key by key, by one warp: o holds
-// its D / 32 columns lane + 32 e, unnormalised; m (log2 units) and l.
+// Rows `todo` (a bit each) of a softmax warp over the piece's key tiles on the
+// CUDA cores, one after the other, 32 keys at a time with the row's true
+// maximum, written in place of what the warp has written.  For the logits kLK
+// lanes take a row of K, 16 bytes each; their sums, kLK of them a lane, are
+// added up and spread out at once (half as many with each exchange), so that
+// lane t of the group g ends with key t * 32 / kLK + g.  For the values a lane
+// takes the D / 32 columns from lane * (D / 32) on, with kAt rows' loads in
+// flight.  Bound by the latency of its loads: 32768 rows over 8192 keys of 128
+// take 31 ms in bf16, 26 in FP8 (264 and 272 with a key at a time and a 5-step
+// shuffle for its logit), where the tensor cores take 0.11 and 0.16.  (Not
+// inlined, with few registers: they are not to weigh on the main loop.)
 template <int KV, int D>
-__device__ __noinline__ void exact_row(const PrefillTCParams& p, const PrefillPiece& pc, int tok, int h, int lane,
-                                       float* o, float& m, float& l) {
-  constexpr int E = D / 32;
-  float q[E], kc[E], vc[E];
+__device__ __noinline__ void exact_rows(const PrefillTCParams& p, const PrefillPiece& pc, int warp, int lane, unsigned todo,
+                                        int* steps) {
+  constexpr int E = D / 32, N = KV == 1 ? 8 : 16, kLK = D / N, kAt = 4;
+  const int t = lane % kLK, mine = t * (32 / kLK) + lane / kLK;
+#pragma unroll 1
+  for (; todo; todo &= todo - 1) {
+    const int r = warp * 32 + __ffs(todo) - 1, tok = r >> p.g_log2;
+    const size_t row_out = (size_t)(pc.q_row + tok) * p.n_heads + (pc.kv_head << p.g_log2) + (r & ((1 << p.g_log2) - 1));
+    float q[N], o[E], m, l;
 #pragma unroll
-  for (int e = 0; e < E; ++e) {
-    const int d = lane + 32 * e;
-    q[e] = __bfloat162float(
-        static_cast<const __nv_bfloat16*>(p.q)[((size_t)(pc.q_row + tok) * p.n_heads + h) * D + d]);
-    o[e] = 0.0f;
-    kc[e] = KV != 1 && p.k_channel != nullptr ? p.k_channel[pc.kv_head * D + d] : 1.0f;
-    vc[e] = KV != 1 && p.v_channel != nullptr ? p.v_channel[pc.kv_head * D + d] : 1.0f;
-  }
-  m = -INFINITY;
-  l = 0.0f;
-  const int i = pc.pos0 + tok, na = tiles_a(pc);
-  for (int k = pc.k0; k < pc.k1; ++k) {
-    int n;
-    const int lb = tile_block(pc, na, k, n);
-    const int hi = min(min((lb + n) * kBlock, pc.ctx_len), i + 1);
-    for (int j = lb * kBlock; j < hi; ++j) {
-      if (!keeps(j, i, p.sinks, p.window)) continue;
-      const size_t r = ((size_t)block_of(p, pc, j / kBlock) * p.n_kv_heads + pc.kv_head) * kBlock + (j & 15);
-      float dot = 0.0f;
+    for (int e = 0; e < N; e += 4) load_values<1, 4>(p.q, row_out * D + t * N + e, q + e);
+    if (KV != 1 && p.k_channel != nullptr) {
 #pragma unroll
-      for (int e = 0; e < E; ++e) dot += q[e] * (stored<KV>(p.k_pool, r * D + lane + 32 * e) * kc[e]);
+      for (int e = 0; e < N; ++e) q[e] *= p.k_channel[pc.kv_head * D + t * N + e];
+    }
 #pragma unroll
-      for (int off = 16; off; off >>= 1) dot += __shfl_xor_sync(kFull, dot, off);
-      const float s = dot * (KV != 1 ? p.k_scale[r] * p.scale : p.scale) * kLog2e;
-      const float mn = fmaxf(m, s);
-      const float pj = s == -INFINITY ? 0.0f : exp2f(s - mn);
-      const float alpha = m == -INFINITY ? 0.0f : exp2f(m - mn);
-      const float w = KV != 1 ? pj * p.v_scale[r] : pj;
-      l = l * alpha + pj;
+    for (int e = 0; e < E; ++e) o[e] = 0.0f;
+    m = -INFINITY;
+    l = 0.0f;  // this lane's keys', until the end
+    const int i = pc.pos0 + tok, na = tiles_a(pc);
+#pragma unroll 1
+    for (int k = pc.k0; k < pc.k1; ++k) {
+      if (lane == 0) atomicAdd(steps, 1);  // waits elsewhere see that this goes on
+      int n;
+      const int lb = tile_block(pc, na, k, n);
+      const int hi = min(min((lb + n) * kBlock, pc.ctx_len), i + 1);
+#pragma unroll 1
+      for (int j0 = lb * kBlock; j0 < hi; j0 += 32) {
+        const bool have = j0 + mine < hi && keeps(j0 + mine, i, p.sinks, p.window);
+        const unsigned counts = __ballot_sync(kFull, have);
+        if (counts == 0) continue;
+        const int j = min(j0 + mine, hi - 1);  // past the last key it is read again, and does not count
+        const unsigned row = ((unsigned)block_of(p, pc, j / kBlock) * p.n_kv_heads + pc.kv_head) * kBlock + (j & 15);
+        const float ks = KV != 1 ? __ldg(p.k_scale + row) : 1.0f, vs = KV != 1 ? __ldg(p.v_scale + row) : 1.0f;
+        float part[kLK];
 #pragma unroll
-      for (int e = 0; e < E; ++e) o[e] = o[e] * alpha + w * (stored<KV>(p.v_pool, r * D + lane + 32 * e) * vc[e]);
-      m = mn;
+        for (int u0 = 0; u0 < kLK; u0 += 4) {
+          uint4 w[4];
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+            w[u] = __ldg(static_cast<const uint4*>(p.k_pool) + (size_t)__shfl_sync(kFull, row, u0 + u, kLK) * kLK + t);
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            float x[N];
+            unpack16<KV>(w[u], x);
+            part[u0 + u] = 0.0f;
+#pragma unroll
+            for (int e = 0; e < N; ++e) part[u0 + u] += q[e] * x[e];
+          }
+          __syncwarp();
+        }
+#pragma unroll
+        for (int half = kLK / 2; half; half /= 2) {
+          const bool high = t & half;
+#pragma unroll
+          for (int u = 0; u < half; ++u)
+            part[u] = (high ? part[u + half] : part[u]) + __shfl_xor_sync(kFull, high ? part[u] : part[u + half], half);
+        }
+        const float s = have ? part[0] * (ks * p.scale) * kLog2e : -INFINITY;
+        float mn = fmaxf(m, s);
+#pragma unroll
+        for (int off = 16; off; off >>= 1) mn = fmaxf(mn, __shfl_xor_sync(kFull, mn, off));
+        const float wk = s == -INFINITY ? 0.0f : exp2f(s - mn), alpha = m == -INFINITY ? 0.0f : exp2f(m - mn);
+        const float wv = wk * vs;
+        l = l * alpha + wk;
+        m = mn;
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] *= alpha;
+#pragma unroll 1
+        for (int u0 = 0; u0 < 32; u0 += kAt) {
+          float v[kAt][E];
+#pragma unroll
+          for (int u = 0; u < kAt; ++u)
+            load_values<KV, E>(p.v_pool, (size_t)__shfl_sync(kFull, row, u0 + u) * D + lane * E, v[u]);
+#pragma unroll
+          for (int u = 0; u < kAt; ++u) {
+            const float wu = __shfl_sync(kFull, wv, u0 + u);
+            if ((counts >> (u0 + u)) & 1) {
+#pragma unroll
+              for (int e = 0; e < E; ++e) o[e] += wu * v[u][e];
+            }
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int off = 16; off; off >>= 1) l += __shfl_xor_sync(kFull, l, off);
+    if (KV != 1 && p.v_channel != nullptr) {
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] *= p.v_channel[pc.kv_head * D + lane * E + e];
+    }
+    if (pc.record >= 0) {
+      float* rec = p.records + (size_t)pc.record * prefill_record_floats(D);
+#pragma unroll
+      for (int e = 0; e < E; ++e) rec[(size_t)r * D + lane * E + e] = o[e];
+      if (lane == 0) {
+        rec[2 * kPreRows * D + r] = m;
+        rec[2 * kPreRows * (D + 1) + r] = l;
+      }
+    } else {
+      const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+#pragma unroll
+      for (int e = 0; e < E; ++e)
+        static_cast<__nv_bfloat16*>(p.out)[row_out * D + lane * E + e] = __float2bfloat16_rn(l == 0.0f ? 0.0f : o[e] * inv);
+      if (lane == 0 && p.lse != nullptr) p.lse[row_out] = row_lse(m, l);
     }
   }
 }
-
-__device__ __forceinline__ float row_lse(float m, float l) { return l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2; }
 
 // The item's output rows from its partial records, by the softmax warps of the
 // CTA that wrote the last one: w_c = 2^(m_c - M), out = sum_c w_c O_c /
 // sum_c w_c l_c, records taken in order.  A warp takes its rows' weights a
 // lane each, then kAt rows' O at a time, whose loads are all in flight.  (Not
-// inlined, like exact_row: their registers are not to weigh on the main loop.)
+// inlined, like exact_rows.)
 template <int D, int kWarps, int kAt>
 __device__ __noinline__ void merge_records(const PrefillTCParams& p, const PrefillPiece& pc, int warp, int lane) {
   constexpr int NV = D / 32;
@@ -1052,22 +1129,8 @@ __device__ void softmax_role(const PrefillTCParams& p, const Ctx<KV, D>& x, uint
         }
       }
     }
-    for (unsigned todo = __ballot_sync(kFull, valid_row && bad != 0.0f); todo; todo &= todo - 1) {
-      const int src = __ffs(todo) - 1, rt = base + src;
-      float o[D / 32], m1, l1;
-      exact_row<KV, D>(p, pc, i * per + (rt >> p.g_log2), (pc.kv_head << p.g_log2) + (rt & ((1 << p.g_log2) - 1)), lane,
-                       o, m1, l1);
-      const float inv1 = l1 == 0.0f ? 0.0f : 1.0f / l1;
-      char* to1 = dst(src);
-#pragma unroll
-      for (int e = 0; e < D / 32; ++e) {
-        if (rec != nullptr)
-          reinterpret_cast<float*>(to1)[lane + 32 * e] = o[e];
-        else
-          reinterpret_cast<__nv_bfloat16*>(to1)[lane + 32 * e] = __float2bfloat16_rn(l1 == 0.0f ? 0.0f : o[e] * inv1);
-      }
-      if (lane == 0) row_stats(src, m1, l1);
-    }
+    const unsigned todo = __ballot_sync(kFull, valid_row && bad != 0.0f);
+    if (todo != 0) exact_rows<KV, D>(p, pc, warp, lane, todo, const_cast<int*>(x.abort + 1));
     if (rec != nullptr) {
       __threadfence();
       __syncwarp();
@@ -1099,14 +1162,14 @@ __global__ void __launch_bounds__(PC<KV, D>::kThreads, 1)
   using C = PC<KV, D>;
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint32_t tmem_at;
-  __shared__ int aborted, last_flag;
+  __shared__ int aborted[2], last_flag;
   Ctx<KV, D> x;
   x.base = (smem_addr(smem_raw) + 1023u) & ~1023u;
-  x.abort = &aborted;
+  x.abort = aborted;
   x.limit_ns = p.wait_limit_ns;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    aborted = 0;
+    aborted[0] = aborted[1] = 0;
     mbar_init(x.q_full(), 1);
     mbar_init(x.q_empty(), 1);
     for (int s = 0; s < C::kStages; ++s) {

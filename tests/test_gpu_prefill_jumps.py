@@ -14,7 +14,7 @@ import math
 import pytest
 import torch
 
-from paged_kv_cache_282_gb300 import PagedKVCache
+from paged_kv_cache_282_gb300 import PagedKVCache, _abi
 from test_gpu_prefill import BF, _run, _stored
 
 pytestmark = pytest.mark.gpu
@@ -101,3 +101,13 @@ def test_values_of_zero_behind_a_rise(kv):
     cache, s = _cache(kv, 128, 640, [(300, 5, 1.0)], size=0.0)
     for jump in JUMPS:
         _jump(cache, s, 140, jump)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8", "int8"])
+def test_such_rows_may_outlast_the_wait_limit(kv):
+    """64 tokens of 8 heads behind 30000 keys, the rise in the last tile, so that every row is computed twice, which takes
+    longer than the waits' limit of 1 ms (as more keys would than the default of 4 s)."""
+    cache, s = _cache(kv, 128, 30000, [(29900, 1, 1.0)])
+    _abi.check(cache.lib.pkv_set_wait_limit(cache.handle, 1_000_000))
+    _jump(cache, s, 64, 50.0)  # ordinary rows take less
+    _jump(cache, s, 64, 100.0)
