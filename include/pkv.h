@@ -299,7 +299,8 @@ pkv_status pkv_prefill_workspace_size(const pkv_pool* pool, size_t* bytes_out);
  * a key of must be present: else PKV_ERR_INVALID_ARG.  PKV_ERR_INVALID_ARG
  * also for more queries than tokens, a scale that is not finite, or when the
  * current device is not the pool's; PKV_ERR_UNSUPPORTED for 2^31 or more query
- * rows, or while `stream` is being captured. */
+ * rows, while `stream` is being captured, or when the tensor-core kernel could
+ * not be set up (a build with other registers than it is made for). */
 pkv_status pkv_prefill_attn(pkv_pool* pool, void* stream, int32_t n_seqs, const int32_t* seq_ids,
                             const int32_t* q_lens, const void* q, float scale, int32_t mask_mode, int32_t num_sinks,
                             int32_t window, void* out, float* lse, void* workspace, size_t workspace_bytes);
@@ -566,6 +567,9 @@ pkv_status pkv_test_starve_next_select(pkv_pool* pool);
  * the wait for it can only run out.  Outputs of that call are undefined; the
  * status word reports PKV_ERR_TIMEOUT. */
 pkv_status pkv_test_starve_next_prefill(pkv_pool* pool);
+/* Test hook: the pool answers as one whose prefill kernel could not be set up
+ * (refuse != 0), or as before (0). */
+pkv_status pkv_test_refuse_prefill(pkv_pool* pool, int32_t refuse);
 /* Test hooks for the decode planner (host only, no device work).
  * pkv_test_set_geometry: the launch geometry a host-only pool plans for --
  * SMs, warps per CTA of the one-sequence and of the two-sequence kernel (one

@@ -108,6 +108,7 @@ SIGNATURES = {
     "pkv_test_starve_next_decode": [c_void_p, c_int32],
     "pkv_test_starve_next_select": [c_void_p],
     "pkv_test_starve_next_prefill": [c_void_p],
+    "pkv_test_refuse_prefill": [c_void_p, c_int32],
     "pkv_test_set_geometry": [c_void_p, c_int32, c_int32, c_int32, c_int32],
     "pkv_test_plan_bytes": [c_void_p, c_int32, c_void_p, c_int32, c_int32, c_int32, c_int32, c_int32, c_void_p,
                             c_size_t, c_void_p, c_void_p],

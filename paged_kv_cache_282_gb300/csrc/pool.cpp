@@ -457,6 +457,7 @@ struct pkv_pool {
   size_t tc_smem = 0;
   CUtensorMap tmap_k{}, tmap_v{};
   CUtensorMap tmap_pk{}, tmap_pv{};  // in groups of 8 rows (prefill, bf16 pools)
+  const char* prefill_refused = nullptr;  // why the tensor-core prefill kernel cannot run here
   bool tc_path = false;
   const float* k_channel = nullptr;  // per-channel scales [Hk][D] (device, borrowed), FP8 / INT8 only
   const float* v_channel = nullptr;
@@ -2321,8 +2322,12 @@ pkv_status pkv_pool_create(const pkv_pool_config* cfg, const pkv_pool_buffers* b
           if (pkv_status r = make_group_map(&p->tmap_pk, b.k_pool, p->cfg)) return fail_dev(r);
           if (pkv_status r = make_group_map(&p->tmap_pv, b.v_pool, p->cfg)) return fail_dev(r);
         }
+        // a pool whose prefill kernel cannot run serves everything else
         e = D == 64 ? prefill_tc_prepare_d64(cfg->kv_dtype) : prefill_tc_prepare_d128(cfg->kv_dtype);
-        if (e != cudaSuccess) return fail_dev(fail(PKV_ERR_CUDA, "prefill kernel setup failed: %s", cudaGetErrorString(e)));
+        if (e != cudaSuccess) {
+          p->prefill_refused = cudaGetErrorString(e);
+          (void)cudaGetLastError();  // not to be taken for a launch's
+        }
         // the plan's warps are the kernel's teams (hg warps each)
         p->tc_ctas_per_sm = std::max(1, occ);
         p->tc_warps_per_cta = tc_teams(cfg->kv_dtype, 1, D, hg);
@@ -3062,6 +3067,8 @@ pkv_status pkv_prefill_attn(pkv_pool* p, void* stream, int32_t n, const int32_t*
     if (pkv_status r = check_call(p, st, "pkv_prefill_attn")) return r;
     PrefillPlan plan;
     const bool tensor = c.kv_dtype != PKV_KV_FP32 && !few_to_prefill(p, n, ids, q_lens, ntok, sinks, window);
+    if (ntok > 0 && tensor && p->prefill_refused)
+      return fail(PKV_ERR_UNSUPPORTED, "the prefill kernel cannot run: %s", p->prefill_refused);
     if (ntok > 0 && tensor) {
       plan_prefill(p, n, ids, q_lens, sinks, window, plan);
       const size_t need = (size_t)plan.records * prefill_record_floats(c.head_dim) * sizeof(float);
@@ -3387,6 +3394,14 @@ pkv_status pkv_test_starve_next_prefill(pkv_pool* p) {
   return guarded([&]() -> pkv_status {
     if (!p) return fail(PKV_ERR_INVALID_ARG, "pool is NULL");
     p->starve_prefill = true;
+    return PKV_OK;
+  });
+}
+
+pkv_status pkv_test_refuse_prefill(pkv_pool* p, int32_t refuse) {
+  return guarded([&]() -> pkv_status {
+    if (!p) return fail(PKV_ERR_INVALID_ARG, "pool is NULL");
+    p->prefill_refused = refuse ? cudaGetErrorString(cudaErrorLaunchOutOfResources) : nullptr;
     return PKV_OK;
   });
 }

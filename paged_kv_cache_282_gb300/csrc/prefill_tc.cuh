@@ -1227,7 +1227,7 @@ __global__ void __launch_bounds__(PC<KV, D>::kThreads, 1)
 }
 
 // The roles' register shares are made for kLaunchRegs: with fewer, a warpgroup
-// would wait for registers that never come free.
+// would wait for registers that never come free.  Such a build is refused.
 template <int KV, int D>
 cudaError_t prefill_prepare_one() {
   using C = PC<KV, D>;
