@@ -2073,7 +2073,7 @@ void plan_prefill(const pkv_pool* p, int32_t n, const int32_t* ids, const int32_
       if (!last_cta && left > 1) {
         const int32_t room = (int32_t)(bound() - at + 0.5) - kPrePieceCost;
         if (room < left) take = std::max(1, room);
-        if (left - take < 2) take = left;  // no piece of one tile
+        if (left - take < 2) take = left;  // no rest of one tile (a CTA with little room left may start with one)
       }
       PrefillPiece pc = it;
       pc.k0 = k;
