@@ -122,7 +122,7 @@ struct Ctx {
   __device__ uint32_t o_full(int i) const { return bar(C::kNumBars - 5 + i); }
   __device__ uint32_t written() const { return bar(C::kNumBars - 3); }  // a piece's partial record
   __device__ uint32_t counted() const { return bar(C::kNumBars - 2); }  // and its merge item's counter
-  __device__ uint32_t idle() const { return bar(C::kNumBars - 1); }     // products done, after a failed wait
+  __device__ uint32_t idle() const { return bar(C::kNumBars - 1); }     // every product is done
 
   // Waits for phase `parity`; false when the limit ran out here or elsewhere
   // in the CTA (every role then leaves).  Rows computed key by key can take
@@ -223,8 +223,9 @@ __device__ __forceinline__ int block_of(const PrefillTCParams& p, const PrefillP
 
 // ---- loads -------------------------------------------------------------------
 
-// Waits, after a failed wait elsewhere, for the copies this warp has in
-// flight: shared memory must not be written after the CTA is gone.
+// Waits for the copies this warp has in flight, before it leaves: a wait that
+// fails elsewhere can end the CTA at any time after that, and shared memory
+// must not be written then.
 template <int KV, int D>
 __device__ void drain(const PrefillTCParams& p, const Ctx<KV, D>& x, int first, int issued, int q_issued, int lane,
                       bool starved = false) {
@@ -328,7 +329,7 @@ __device__ void load_role(const PrefillTCParams& p, const Ctx<1, D>& x, int firs
     }
   }
   if (IS_V && ok) ok = zero_tail();
-  if (!ok) drain(p, x, IS_V ? 1 : 0, issued, pieces, lane, starve);
+  drain(p, x, IS_V ? 1 : 0, issued, pieces, lane, starve);
 }
 
 // One-byte pools: one warp loads the queries only.
@@ -344,7 +345,7 @@ __device__ void query_role(const PrefillTCParams& p, const Ctx<KV, D>& x, int fi
     load_q(p, x, pc, lane);
     ++pieces;
   }
-  if (!ok) drain(p, x, 0, 0, pieces, lane);
+  drain(p, x, 0, 0, pieces, lane);
 }
 
 // One-byte pools: one warp brings the tiles' scales, the keys' times the
@@ -484,10 +485,10 @@ __device__ void product_role(const PrefillTCParams& p, const Ctx<KV, D>& x, uint
       now[1] = then[1];
     }
   }
-  if (!ok) {  // tensor memory is freed only when nothing uses it any more
-    mma_commit(x.idle());
-    if (!mbar_wait(x.idle(), 0, kDrainNs)) atomicOr(p.status, kStatusUndrained);
-  }
+  // tensor memory is freed only when nothing uses it any more (the softmax may
+  // have left after a failed wait)
+  mma_commit(x.idle());
+  if (!mbar_wait(x.idle(), 0, kDrainNs)) atomicOr(p.status, kStatusUndrained);
 }
 
 // ---- widening one-byte codes ---------------------------------------------------
