@@ -281,14 +281,13 @@ pkv_status pkv_prefill_workspace_size(const pkv_pool* pool, size_t* bytes_out);
  *   s_j = scale * q . K_j,  out = sum_j softmax(s)_j V_j,  lse = ln sum_j exp(s_j)
  * A query that keeps no key (or only keys of weight zero) gives out = 0,
  * lse = -inf.  A key that a query does not keep does not reach its result,
- * whatever its K and V hold (next to a NaN or an infinity in V, or where its
- * logits rise by more than about 80 from one 128 keys to the next, a query
- * may be evaluated key by key: the same result up to rounding, a query some
- * hundred times slower).  Accumulation,
- * softmax and lse are fp32; on the tensor cores (every pool but fp32) each
- * weight, times its V scale, is rounded to bf16 for the product with V, but
- * not in a call of at most 1024 query rows (tokens times heads) of which none
- * keeps more than 64 keys.
+ * whatever its K and V hold (next to a NaN or an infinity, or where its logits
+ * rise by more than about 80 from one 128 keys to the next, a query may be
+ * evaluated key by key: the same result up to rounding, but a query then takes
+ * some hundred times longer).  Accumulation, softmax and lse are fp32; on the
+ * tensor cores (every pool but fp32) each weight, times its V scale, is rounded
+ * to bf16 for the product with V, but not in a call of at most 1024 query rows
+ * (tokens times heads) of which none keeps more than 64 keys.
  *   q, out     device [token][n_heads][D] (fp32 for fp32 pools, else bf16),
  *              16-byte aligned, not overlapping
  *   lse        device [token][n_heads] fp32, or NULL

@@ -393,7 +393,9 @@ class PagedKVCache:
                 window: int = 0, out=None, lse=None, workspace=None, stream=None):
         """Attention of each listed sequence's last q_lens[i] tokens over its
         cached keys, causal; q: [sum(q_lens)][n_heads][head_dim], packed.
-        Returns (out, lse); lse=False leaves it out."""
+        Returns (out, lse); lse=False leaves it out.  workspace: a tensor of
+        prefill_workspace_bytes() bytes that no other call uses meanwhile
+        (default: one of the stream's own)."""
         import torch
         dt, dev = self._row_dtype, self.k_pool.device
         ids, lens = _i32_array(seq_ids), _i32_array(q_lens)
@@ -412,6 +414,8 @@ class PagedKVCache:
             raise ValueError(f"lse must be contiguous float32 [{n}][{self.n_heads}] on {dev}")
         if scale is None:
             scale = 1.0 / math.sqrt(self.head_dim)
+        if workspace is not None and (workspace.device != dev or not workspace.is_contiguous()):
+            raise ValueError(f"workspace must be contiguous, on {dev}")
         at = _stream_ptr(stream)
         ws = workspace if workspace is not None else self._prefill_workspace(at, stream)
         _abi.check(self.lib.pkv_prefill_attn(

@@ -91,3 +91,16 @@ def test_prefill_scratch_belongs_to_the_stream(monkeypatch):
     c.append_rope([0], k, k, rope, counts=[2], q=q, stream=streams[0])
     c.qk_norm_rope(q, k, None, rope, stream=streams[1])
     assert [s.cuda_stream for s in made] == [1, 1, 1, 2, 2, 2, 1, 1, 2, 2, 1, 2, 2]
+
+
+def test_prefill_refuses_a_workspace_that_the_kernel_cannot_use():
+    c = _cache("pkv_prefill_attn")
+    q = torch.zeros(2, H, D, dtype=BF)
+    kw = dict(out=torch.zeros_like(q), lse=False, stream=STREAM)
+    for bad in (torch.empty(1 << 20, dtype=torch.uint8, device="meta"), torch.empty(1 << 20, dtype=torch.uint8)[::2]):
+        with pytest.raises(ValueError):
+            c.prefill([0], [2], q, workspace=bad, **kw)
+    assert not c.lib.calls
+    good = torch.empty(1 << 20, dtype=torch.float32)
+    c.prefill([0], [2], q, workspace=good, **kw)
+    assert c.lib.calls[0][1][12:] == (good.data_ptr(), 4 << 20)
