@@ -21,10 +21,12 @@
 // What bounds it: in bf16 the chain of a query tile, S -> P (about 1300 clocks
 // with the other tile's threads beside it) -> O and the next S (1024 clocks of
 // products, 2048 with the other tile's): an 8192-token prompt of 32 / 8 heads of
-// 128 takes 361 us, 1520 TFLOP/s at 2070 MHz.  In one-byte pools the issue
-// slots: softmax and widening take 2950 of them per key tile and SM quarter,
-// where the products take 2048 clocks; 2048 tokens at 30719 in an FP8 pool
-// take 986 us, 1080 TFLOP/s.
+// 128 takes 364 us, 1510 TFLOP/s at 2070 MHz.  In one-byte pools no unit is full
+// either (FP8: issue slots 55 % busy, tensor pipe 41 %; INT8 at D = 64: 47 % and
+// 18 %): a key tile takes 4900 clocks, 2048 of products (D = 64: 4600, 1024), in
+// the same chain, with widening beside the exponentials and on fewer registers.
+// Which wait of it is the longest has not been told apart.  2048 tokens at
+// 30719 in an FP8 pool take 988 us, 1077 TFLOP/s.
 //
 // The order of issue, PV_i(k) then QK_i(k + 1), makes the arrival of S_i(k + 1)
 // also say that O_i holds tile k.  A row's reference m is known before the
@@ -90,7 +92,8 @@ struct PC {
   static constexpr int kBytes = 1024 + kBars + kNumBars * 8;
   static_assert(kBytes + 64 <= 232448, "shared memory of a CTA");
   // registers per thread: softmax (more than the launch gives), then products
-  // and loads, and widening (fewer)
+  // and loads, and widening (fewer).  In one-byte pools they do not quite hold
+  // the softmax: 100 bytes are spilled at D = 128, 36 at D = 64.
   static constexpr int kSoftRegs = kOneByte ? 144 : 208, kIssueRegs = kOneByte ? 64 : 88, kWidenRegs = 64;
   static constexpr int kLaunchRegs = 65536 / kThreads / 8 * 8;
   static_assert(kSoftRegs > kLaunchRegs && kIssueRegs < kLaunchRegs && kWidenRegs < kLaunchRegs, "");
@@ -877,6 +880,8 @@ __device__ __forceinline__ uint32_t kept_bits(int from, int past, int win, int s
 __device__ __forceinline__ void load_pairs(uint32_t at, uint64_t& a, uint64_t& b) {
   asm("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(a), "=l"(b) : "r"(at));
 }
+// log2 x on the hardware approximation: only moves the reference, whose step
+// the row's factor follows, so that its error cancels.
 __device__ __forceinline__ float hw_log2(float x) {
   float y;
   asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -1028,6 +1033,12 @@ __device__ void softmax_role(const PrefillTCParams& p, const Ctx<KV, D>& x, uint
             unpack2(mul2(pack2(a[j], a[j + 1]), g01), a[j], a[j + 1]);
             unpack2(mul2(pack2(a[j + 2], a[j + 3]), g23), a[j + 2], a[j + 3]);
           }
+          // Rounded to bf16 (by 2^-8 at most), as both operands of a product have
+          // one type and V is bf16 or codes widened to it: the result's error
+          // against 64 bits grows from 0.0017 (its own rounding) to 0.0023.  fp16,
+          // which codes would fit, holds no weight above 65504, and here they grow
+          // with the logits until the reference moves; a second product with what
+          // the rounding drops would make three products of two.
           w[j / 2] = bf16_pair(a[j], a[j + 1]);
           w[j / 2 + 1] = bf16_pair(a[j + 2], a[j + 3]);
         }
