@@ -15,7 +15,7 @@ import pytest
 import torch
 
 from paged_kv_cache_282_gb300 import PagedKVCache, _abi
-from test_gpu_prefill import BF, _run, _stored
+from test_gpu_prefill import BF, _kept, _pool, _q, _run, _stored
 
 pytestmark = pytest.mark.gpu
 
@@ -37,11 +37,11 @@ def _cache(kv, D, L, at, size=0.1):
     return cache, s
 
 
-def _check(cache, s, q, out, lse, scale):
+def _check(cache, s, q, out, lse, scale, mask="full", S=0, W=0):
     G, D, T = cache.group, cache.head_dim, q.shape[0]
     k, v = (x.repeat_interleave(G, 1) for x in _stored(cache, s))
     L = k.shape[0]
-    keep = torch.arange(L, device="cuda")[None] <= torch.arange(L - T, L, device="cuda")[:, None]
+    keep = _kept(mask, S, W, torch.arange(L - T, L, device="cuda")[:, None], torch.arange(L, device="cuda")[None])
     lg = (torch.einsum("thd,jhd->htj", q.double(), k) * scale).masked_fill(~keep, -math.inf)
     mag = (torch.einsum("thd,jhd->htj", q.double().abs(), k.abs()) * abs(scale)).masked_fill(~keep, 0.0)
     p = torch.softmax(lg, -1)
@@ -111,3 +111,16 @@ def test_such_rows_may_outlast_the_wait_limit(kv):
     _abi.check(cache.lib.pkv_set_wait_limit(cache.handle, 1_000_000))
     _jump(cache, s, 64, 50.0)  # ordinary rows take less
     _jump(cache, s, 64, 100.0)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8", "int8"])
+@pytest.mark.parametrize("G,D", [(1, 128), (2, 64), (8, 128), (8, 64)])
+@pytest.mark.parametrize("mask,S,W", [("full", 0, 0), ("sliding", 0, 200), ("sink_window", 20, 333)])
+@pytest.mark.parametrize("L,T", [(700, 200), (9000, 5)])
+def test_random_logits_of_a_wide_range(kv, G, D, mask, S, W, L, T):
+    """Logits with a deviation of 100, so that rows rise in some tiles and not in others; per-channel scales."""
+    cache, ids = _pool(kv, 2 * G, 2, D, [L], seed=G, channel=kv != "bf16")
+    q = _q(cache, T, seed=D)
+    scale = 100.0 / float(torch.einsum("thd,jhd->htj", q[:50].double(), _stored(cache, ids[0])[0][:50].repeat_interleave(G, 1)).std())
+    out, lse = _run(cache, ids, [T], q, scale=scale, mask=mask, num_sinks=S, window=W)
+    _check(cache, ids[0], q, out, lse, scale, mask, S, W)
